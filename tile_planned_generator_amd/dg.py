@@ -380,6 +380,15 @@ def _rows2(t, name, rows, cols, dtypes, device):
     return ld
 
 
+def _experts(t, name):
+    """Check the experts' stride of an operand; returns it.  (The library takes 0 for
+    tightly packed: one copy expanded over the experts would be read past its end.)"""
+    step = t.stride(0)
+    if step == 0 and t.shape[0] > 1:
+        raise ValueError(f"{name} is one copy expanded over the experts; each expert needs its own")
+    return step
+
+
 def _flat(t, name, count, dtype, device):
     """Check a contiguous index or weight array of `count` entries."""
     if t.dtype != dtype or t.numel() != count or not t.is_contiguous() or t.device != device:
@@ -558,8 +567,9 @@ class Handle:
         """The experts' products through dg_gemm_fp8_grouped: rows offsets[e] ..
         offsets[e+1]-1 of C_out [R, N] = those of A [R, K] times B[e]^T.
 
-        B [E, N, K] codes, SB [E, ceil(K/128), ceil(N/128)], SA [ceil(K/128), R],
-        offsets int32 [E + 1].  Rows in no segment are not written.
+        B [E, N, K] codes, SB [E, ceil(K/128), ceil(N/128)] (neither expanded over
+        E), SA [ceil(K/128), R], offsets int32 [E + 1].  Rows in no segment are not
+        written.
         """
         ty = _types()
         dev, codes, types = A.device, ty.codes, ty.move
@@ -574,8 +584,9 @@ class Handle:
         if E == 0:
             return
         ldb, lsb = _rows2(B[0], "B[e]", N, K, codes, dev), _rows2(SB[0], "SB[e]", kb, nb, ty.only_f32, dev)
+        xb, xs = _experts(B, "B"), _experts(SB, "SB")
         check(dg_gemm_fp8_grouped(self.h, R, N, K, E, A.data_ptr(), lda, SA.data_ptr(), lsa, B.data_ptr(), ldb,
-                                  B.stride(0), SB.data_ptr(), lsb, SB.stride(0), offsets.data_ptr(),
+                                  xb, SB.data_ptr(), lsb, xs, offsets.data_ptr(),
                                   C_out.data_ptr(), types[C_out.dtype], ldc, _stream(dev, stream)))
 
     def gemm_fp8_wgrad(self, A, SA, B, SB, offsets, C_out, *, stream=None):
