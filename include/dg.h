@@ -455,7 +455,8 @@ dg_status dg_gemm_fp8_grouped(dg_handle_t h, int64_t rows, int64_t N, int64_t K,
  * quantised down the columns (dg_quant_fp8 with transpose 1): scales
  * [ceil(rows/128)][lda_scale >= M] and [..][ldb_scale >= N].  offsets start on multiples
  * of 128 (dg_moe_sort with align 128); other starts are taken as the multiple
- * below.  An expert without rows gets zeros. */
+ * below.  An expert without rows gets zeros.  The experts' matrices of C share no
+ * element (one after the other, or their rows side by side inside ldc). */
 dg_status dg_gemm_fp8_wgrad(dg_handle_t h, int64_t M, int64_t N, int64_t rows, int64_t experts, const void *A,
                             int64_t lda, const float *a_scale, int64_t lda_scale, const void *B, int64_t ldb,
                             const float *b_scale, int64_t ldb_scale, const int32_t *offsets, void *C, int32_t c_type,

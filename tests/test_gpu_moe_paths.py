@@ -1,0 +1,30 @@
+"""GPU: calls of the 8-bit expert layer that other tests do not reach, and what they
+refuse on a device.  Formulas in 64 bits and bounds as in tests/moe_ref.py."""
+import pytest
+import torch
+
+from tests.parity import say
+from tests.test_gpu_moe import DEV, codes, gen, h, scales  # noqa: F401 (h: fixture)
+from tile_planned_generator_amd import dg
+
+pytestmark = pytest.mark.gpu
+
+
+def test_weight_gradients_that_share_elements_are_refused(h):
+    """Before anything is enqueued: C keeps what it held."""
+    say("[case] wgrad, overlapping experts")
+    g = gen(71)
+    M, N, R, E = 64, 80, 256, 2
+    a, b, sa, sb = codes(g, M, R), codes(g, N, R), scales(g, 2, M), scales(g, 2, N)
+    off = torch.tensor([0, 128, 256], dtype=torch.int32, device=DEV)
+    flat = torch.full((2 * M * N,), 7.0, device=DEV)
+    for stride in (N, M * N - 1):
+        with pytest.raises(dg.DGError) as e:
+            h.gemm_fp8_wgrad(a, sa, b, sb, off, flat.as_strided((E, M, N), (stride, N, 1)))
+        assert e.value.status == dg.DG_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (flat == 7).all()
+    one, side = torch.empty(E, M, N, device=DEV), torch.empty(M, E, N, device=DEV)
+    h.gemm_fp8_wgrad(a, sa, b, sb, off, one)
+    h.gemm_fp8_wgrad(a, sa, b, sb, off, side.transpose(0, 1))   # the experts' rows side by side
+    assert torch.equal(one, side.transpose(0, 1))

@@ -6,6 +6,7 @@
 
 #include "api_internal.h"
 #include "dg_args.h"
+#include "fp8_rules.h"
 #include "launch.h"
 #include "moe_args.h"
 
@@ -297,6 +298,8 @@ dg_status dg_gemm_fp8_wgrad(dg_handle_t h, int64_t M, int64_t N, int64_t rows, i
         if (la < rows || lb < rows || lc < N || lsa < M || lsb < N)
             return api_fail(DG_ERR_INVALID_ARG, "a leading dimension is smaller than the matrix");
         if (M == 0 || N == 0 || experts == 0) return DG_OK;
+        if (!experts_disjoint(M, N, lc, xc, experts))
+            return api_fail(DG_ERR_INVALID_ARG, "the experts' matrices of C share elements");
         if (!offsets) return api_fail(DG_ERR_INVALID_ARG, "offsets are required");
         Fp8Args a{};
         DG_TRY(check_out(C, c_type, a.out_type));

@@ -382,7 +382,8 @@ def _rows2(t, name, rows, cols, dtypes, device):
 
 def _experts(t, name):
     """Check the experts' stride of an operand; returns it.  (The library takes 0 for
-    tightly packed: one copy expanded over the experts would be read past its end.)"""
+    tightly packed: one copy expanded over the experts would be read, or written, past
+    its end.)"""
     step = t.stride(0)
     if step == 0 and t.shape[0] > 1:
         raise ValueError(f"{name} is one copy expanded over the experts; each expert needs its own")
@@ -594,7 +595,8 @@ class Handle:
         A[:, seg] . B[:, seg]^T, seg the rows offsets[e] .. offsets[e+1]-1.
 
         A [M, R], B [N, R] codes quantised down the columns, SA [ceil(R/128), M], SB
-        [ceil(R/128), N], offsets int32 [E + 1] on multiples of 128.
+        [ceil(R/128), N], offsets int32 [E + 1] on multiples of 128; C_out's experts
+        share no element.
         """
         ty = _types()
         dev, codes, types = A.device, ty.codes, ty.move
@@ -609,10 +611,10 @@ class Handle:
         _flat(offsets, "offsets", E + 1, ty.i32, dev)
         if E == 0:
             return
-        ldc = _rows2(C_out[0], "C[e]", M, N, types, dev)
+        ldc, xc = _rows2(C_out[0], "C[e]", M, N, types, dev), _experts(C_out, "C")
         check(dg_gemm_fp8_wgrad(self.h, M, N, R, E, A.data_ptr(), lda, SA.data_ptr(), lsa, B.data_ptr(), ldb,
                                 SB.data_ptr(), lsb, offsets.data_ptr(), C_out.data_ptr(), types[C_out.dtype], ldc,
-                                C_out.stride(0), _stream(dev, stream)))
+                                xc, _stream(dev, stream)))
 
     def moe_sort_workspace(self, tokens, topk, experts):
         """Bytes of workspace moe_sort needs (dg_moe_sort_workspace)."""
