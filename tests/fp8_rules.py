@@ -12,6 +12,7 @@ SHIM = """
 extern "C" {
 int experts_disjoint(int64_t M, int64_t N, int64_t ld, int64_t stride, int64_t experts)
 { return dg::experts_disjoint(M, N, ld, stride, experts); }
+int rows_fit_32(int rows, int64_t ld, int64_t K) { return dg::rows_fit_32(rows, ld, K); }
 }
 """
 
@@ -25,4 +26,5 @@ def lib():
         subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I" + CSRC, src, "-o", so], check=True)
         loaded = C.CDLL(so)
     loaded.experts_disjoint.argtypes = [C.c_int64] * 5
+    loaded.rows_fit_32.argtypes = [C.c_int, C.c_int64, C.c_int64]
     return loaded

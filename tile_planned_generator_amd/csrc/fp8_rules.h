@@ -15,4 +15,13 @@ inline bool experts_disjoint(int64_t M, int64_t N, int64_t ld, int64_t stride, i
     return stride >= span || (stride >= N && ld >= (__int128)(experts - 1) * stride + N);
 }
 
+// Whether every byte of `rows` rows of K bytes, ld apart, has an offset below 2^32: the
+// kernels count bytes from a tile's origin in 32 bits.  (Divided, as ld * rows may
+// pass 64 bits: pitches from 2^57 on would look small.)
+inline bool rows_fit_32(int rows, int64_t ld, int64_t K)
+{
+    const int64_t last = (int64_t(1) << 32) - 1;
+    return K <= last && ld <= (last - K) / rows;
+}
+
 }  // namespace dg

@@ -119,7 +119,7 @@ dg_status check_operands(const void *A, int64_t lda, const float *sa, const void
     if (!aligned(A, 16) || !aligned(B, 16) || lda % 16 || ldb % 16)
         return api_fail(DG_ERR_ALIGNMENT, "A and B: 16-byte aligned pointers and rows");
     if (!aligned(sa, 4) || !aligned(sb, 4)) return api_fail(DG_ERR_ALIGNMENT, "scale arrays are 4-byte aligned");
-    if (lda * 128 + K >= (int64_t(1) << 32) || ldb * 128 + K >= (int64_t(1) << 32))
+    if (!rows_fit_32(128, lda, K) || !rows_fit_32(128, ldb, K))
         return api_fail(DG_ERR_UNSUPPORTED, "128 rows of an operand span 4 GiB or more");
     return DG_OK;
 }
