@@ -6,9 +6,10 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "fp8_rules.h"
+
 namespace dg {
 
-constexpr int FP8_BLOCK = 128;       // values along K that share a scale
 constexpr int MOE_MAX_EXPERTS = 512;
 
 // Block-scaled fp8 product of A [M][K] and B [N][K] (K contiguous in both):
@@ -32,8 +33,6 @@ struct Fp8Args {
     int split_k, k_slice;            // FP8_DENSE: K slices (k_slice a multiple of 128) into ws [split][M][N]
     float *ws;
 };
-// Kernel variants of the product (indices of the tables in gemm_fp8.hip).
-enum Fp8Kernel : int { FP8_STREAM16 = 0, FP8_TILE64, FP8_TILE128, FP8_TILE256, FP8_KERNELS };
 struct Fp8Shape {
     int bm, bn, threads;
     bool stream;                     // K is cut over the waves of a workgroup
