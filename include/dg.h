@@ -414,9 +414,10 @@ dg_status dg_quant_fp8(dg_handle_t h, int64_t rows, int64_t cols, const void *X,
                        int64_t ldx, const int32_t *index, int32_t index_div, int32_t transpose, void *codes,
                        int64_t ldq, float *scales, int64_t ld_scale, dg_stream_t stream);
 
-/* The kernel dg_gemm_fp8 takes for a problem with a 16-bit C (an F32 C takes 128 x 128
- * tiles where this says 256 x 256), its tile, its K split and the workspace it
- * needs, the same for every C (the estimates are 0: the kernel is chosen by rule). */
+/* The kernel dg_gemm_fp8 takes for a problem with a 16-bit C (an F32 C, or an operand
+ * whose rows lie about 16 MiB or more apart, takes 128 x 128 tiles where this says 256 x
+ * 256), its tile, its K split and the workspace it needs, the same for every C (the
+ * estimates are 0: the kernel is chosen by rule). */
 dg_status dg_plan_fp8(dg_handle_t h, int64_t M, int64_t N, int64_t K, dg_plan_info *out);
 
 /* Block-scaled product

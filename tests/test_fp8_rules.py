@@ -19,8 +19,7 @@ def test_rows_whose_offsets_fit_32_bits(rows):
 
 
 def test_kernel_of_each_size():
-    r = fp8_rules.lib()
-    dense, rows, wgrad = r.choose_dense, r.choose_rows, r.choose_wgrad
+    dense, rows, wgrad = fp8_rules.dense, fp8_rules.rows, fp8_rules.wgrad
     S, T64, T128, T256 = fp8_rules.STREAM16, fp8_rules.TILE64, fp8_rules.TILE128, fp8_rules.TILE256
     for exact in (0, 1):
         assert [dense(M, 4096, 4096, exact) for M in (1, 16, 17, 512, 1024)] == [S, S, T64, T64, T128]
@@ -29,3 +28,15 @@ def test_kernel_of_each_size():
         assert [wgrad(256, 256, n, exact) for n in (8, 64)] == [T64, T128]
         assert wgrad(256, 256, 256, exact) == (T128 if exact else T256)
     assert [rows(n, 8, 4096, 1) for n in (1, 32)] == [S, S] and rows(32, 8, 4096, 0) == T64
+
+
+@pytest.mark.parametrize("which", ["lda", "ldb"])
+def test_wide_rows_leave_the_256_tile(which):
+    """255 rows of a pitch from 2^24 on pass 32 bits, where the 128 x 128 tile's do not."""
+    dense, rows, wgrad = fp8_rules.dense, fp8_rules.rows, fp8_rules.wgrad
+    for ld, tile in ((2 ** 24 - 16, fp8_rules.TILE256), (2 ** 24, fp8_rules.TILE128), (20 << 20, fp8_rules.TILE128),
+                     (2 ** 25 - 16, fp8_rules.TILE128)):
+        assert dense(256, 49152, 1, 0, **{which: ld}) == tile
+        assert rows(256, 1, 49152, 0, **{which: ld}) == tile
+        assert wgrad(256, 256, 192, 0, **{which: ld}) == tile
+    assert dense(256, 49152, 2 ** 24 - 16, 0, lda=2 ** 24 - 16, ldb=2 ** 24 - 16) == fp8_rules.TILE128   # (K counts too)

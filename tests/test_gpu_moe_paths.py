@@ -3,8 +3,9 @@ refuse on a device.  Formulas in 64 bits and bounds as in tests/moe_ref.py."""
 import pytest
 import torch
 
+from tests import moe_ref as ref
 from tests.parity import say
-from tests.test_gpu_moe import DEV, codes, gen, h, scales  # noqa: F401 (h: fixture)
+from tests.test_gpu_moe import DEV, F8, check_product, codes, gen, h, scales  # noqa: F401 (h: fixture)
 from tile_planned_generator_amd import dg
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,22 @@ def test_weight_gradients_that_share_elements_are_refused(h):
     h.gemm_fp8_wgrad(a, sa, b, sb, off, one)
     h.gemm_fp8_wgrad(a, sa, b, sb, off, side.transpose(0, 1))   # the experts' rows side by side
     assert torch.equal(one, side.transpose(0, 1))
+
+
+def test_rows_20_mib_apart(h):
+    """The size takes the 256 x 256 tile, 255 of whose rows would lie past 4 GiB."""
+    M, N, K, ld = 256, 49152, 128, 20 << 20
+    say(f"[case] gemm_fp8 {M}x{N}x{K}, rows of A {ld} bytes apart")
+    g = gen(72)
+    a = torch.empty((M - 1) * ld + K, dtype=torch.uint8, device=DEV).view(F8).as_strided((M, K), (ld, 1))
+    near = codes(g, M, K)
+    a.copy_(near)
+    b, sa, sb = codes(g, N, K), scales(g, 1, M), scales(g, 1, N // 128)
+    c, want = (torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    h.gemm_fp8(a, sa, b, sb, c)
+    h.gemm_fp8(near, sa, b, sb, want)
+    da, db = ref.dequant(near.cpu(), sa.cpu()), ref.dequant(b.cpu(), sb.cpu(), 128)
+    exact, mag = ref.product(da, db)
+    unit = ref.unit_error(da, db)
+    check_product(c, exact, mag, K, unit)
+    check_product(want, exact, mag, K, unit)

@@ -112,7 +112,7 @@ dg_status dg_plan_fp8(dg_handle_t h, int64_t M, int64_t N, int64_t K, dg_plan_in
         if (!api_live(h)) return api_fail(DG_ERR_INVALID_STATE, "handle is NULL or destroyed");
         DG_TRY(sizes_ok({M, N, K}));
         if (!out) return api_fail(DG_ERR_INVALID_ARG, "out is NULL");
-        const Fp8Choice c = choose_dense(M, N, K, false);
+        const Fp8Choice c = choose_dense(M, N, K, huge_tile(false, K, K, K));
         const Fp8Shape &s = fp8_shape(c.kernel);
         dg_plan_info i{};
         i.path = s.stream ? DG_PATH_SKINNY : DG_PATH_TILED;
@@ -156,7 +156,7 @@ dg_status dg_gemm_fp8(dg_handle_t h, int64_t M, int64_t N, int64_t K, const void
         Fp8Args a{};
         DG_TRY(check_out(C, c_type, a.out_type));
         if (K > 0) DG_TRY(check_operands(A, la, a_scale, B, lb, b_scale, K));
-        const Fp8Choice c = choose_dense(M, N, K, a.out_type == T_F32);
+        const Fp8Choice c = choose_dense(M, N, K, huge_tile(a.out_type == T_F32, la, lb, K));
         slices(K, c.split, a.k_slice, a.split_k);
         if (a.split_k > 1) {
             const size_t need = (size_t)a.split_k * M * N * 4;
@@ -208,7 +208,9 @@ dg_status dg_gemm_fp8_grouped(dg_handle_t h, int64_t rows, int64_t N, int64_t K,
         a.A = A, a.B = B, a.sa = a_scale, a.sb = b_scale, a.C = C, a.off = offsets;
         a.lda = la, a.ldb = lb, a.ld_sa = lsa, a.ld_sb = lsb, a.ldc = lc, a.stride_b = xb, a.stride_sb = xs;
         a.M = (int)rows, a.N = (int)N, a.K = (int)K, a.experts = (int)experts, a.split_k = 1;
-        return launched(launch_fp8(choose_rows(rows, experts, N, a.out_type == T_F32), FP8_ROWS, FP8_BLOCK, a, reinterpret_cast<hipStream_t>(stream)));
+        const bool exact = a.out_type == T_F32;
+        return launched(launch_fp8(choose_rows(rows, experts, N, exact, huge_tile(exact, la, lb, K)), FP8_ROWS, FP8_BLOCK,
+                                   a, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return api_fail(DG_ERR_INTERNAL, "exception in dg_gemm_fp8_grouped");
     }
@@ -240,7 +242,8 @@ dg_status dg_gemm_fp8_wgrad(dg_handle_t h, int64_t M, int64_t N, int64_t rows, i
         a.A = A, a.B = B, a.sa = a_scale, a.sb = b_scale, a.C = C, a.off = offsets;
         a.lda = la, a.ldb = lb, a.ld_sa = lsa, a.ld_sb = lsb, a.ldc = lc, a.stride_c = xc;
         a.M = (int)M, a.N = (int)N, a.K = (int)rows, a.experts = (int)experts, a.split_k = 1;
-        return launched(launch_fp8(choose_wgrad(M, N, experts, a.out_type == T_F32), FP8_WGRAD, 1, a, reinterpret_cast<hipStream_t>(stream)));
+        return launched(launch_fp8(choose_wgrad(M, N, experts, huge_tile(a.out_type == T_F32, la, lb, rows)), FP8_WGRAD, 1,
+                                   a, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return api_fail(DG_ERR_INTERNAL, "exception in dg_gemm_fp8_wgrad");
     }
