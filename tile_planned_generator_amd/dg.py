@@ -314,13 +314,14 @@ def _dtype_name(t):
             torch.int32: "i32"}[t.dtype]
 
 
-def _stream(device, stream):
-    """The HIP stream of a call: `stream`, or the current stream of `device`."""
-    if stream is not None:
-        return stream
+def _stream(h, device, stream):
+    """The HIP stream of a call through handle h: `stream`, or the current stream of
+    the operands' `device`, which has to be the handle's."""
     if device.type != "cuda":
         raise ValueError(f"the operands are on {device}, not on a GPU")
-    return _types().current_stream(device.index)
+    if h.index is not None and device.index != h.index:
+        raise ValueError(f"the operands are on {device}, the handle is cuda:{h.index}'s")
+    return _types().current_stream(device.index) if stream is None else stream
 
 
 def _ptr(t):
@@ -412,9 +413,11 @@ class Handle:
     def __init__(self, device=None, offline=None):
         self.h = C.c_void_p()
         if offline is not None:
+            self.index = None
             check(dg_create_offline(C.byref(self.h), C.byref(offline)))
         else:
-            check(dg_create(C.byref(self.h), 0 if device is None else int(device)))
+            self.index = 0 if device is None else int(device)
+            check(dg_create(C.byref(self.h), self.index))
 
     def close(self):
         if self.h:
@@ -528,7 +531,7 @@ class Handle:
         ldq = _rows2(codes, "codes", m, n, ty.codes, dev)
         lds = _rows2(scales, "scales", -(-n // 128), m, ty.only_f32, dev)
         check(dg_quant_fp8(self.h, R, K, X.data_ptr(), types[X.dtype], T, ldx, _ptr(index), index_div,
-                           int(transpose), codes.data_ptr(), ldq, scales.data_ptr(), lds, _stream(dev, stream)))
+                           int(transpose), codes.data_ptr(), ldq, scales.data_ptr(), lds, _stream(self, dev, stream)))
 
     def plan_fp8(self, M, N, K):
         """The kernel, K split and workspace of a dg_gemm_fp8 problem."""
@@ -555,14 +558,14 @@ class Handle:
         lsa = _rows2(SA, "SA", kb, M, ty.only_f32, dev)
         lsb = _rows2(SB, "SB", kb, -(-N // b_block), ty.only_f32, dev)
         ldc = _rows2(C_out, "C", M, N, types, dev)
+        on = _stream(self, dev, stream)
         if workspace is None:
             need = self.plan_fp8(M, N, K).workspace_bytes
             if need:
                 workspace = ty.space(need, dev, stream)
         wsb = _space(workspace, dev)
         check(dg_gemm_fp8(self.h, M, N, K, A.data_ptr(), lda, SA.data_ptr(), lsa, B.data_ptr(), ldb, SB.data_ptr(),
-                          lsb, b_block, C_out.data_ptr(), types[C_out.dtype], ldc, _ptr(workspace), wsb,
-                          _stream(dev, stream)))
+                          lsb, b_block, C_out.data_ptr(), types[C_out.dtype], ldc, _ptr(workspace), wsb, on))
 
     def gemm_fp8_grouped(self, A, SA, B, SB, offsets, C_out, *, stream=None):
         """The experts' products through dg_gemm_fp8_grouped: rows offsets[e] ..
@@ -588,7 +591,7 @@ class Handle:
         xb, xs = _experts(B, "B"), _experts(SB, "SB")
         check(dg_gemm_fp8_grouped(self.h, R, N, K, E, A.data_ptr(), lda, SA.data_ptr(), lsa, B.data_ptr(), ldb,
                                   xb, SB.data_ptr(), lsb, xs, offsets.data_ptr(),
-                                  C_out.data_ptr(), types[C_out.dtype], ldc, _stream(dev, stream)))
+                                  C_out.data_ptr(), types[C_out.dtype], ldc, _stream(self, dev, stream)))
 
     def gemm_fp8_wgrad(self, A, SA, B, SB, offsets, C_out, *, stream=None):
         """The experts' weight gradients through dg_gemm_fp8_wgrad: C_out[e] [M, N] =
@@ -614,7 +617,7 @@ class Handle:
         ldc, xc = _rows2(C_out[0], "C[e]", M, N, types, dev), _experts(C_out, "C")
         check(dg_gemm_fp8_wgrad(self.h, M, N, R, E, A.data_ptr(), lda, SA.data_ptr(), lsa, B.data_ptr(), ldb,
                                 SB.data_ptr(), lsb, offsets.data_ptr(), C_out.data_ptr(), types[C_out.dtype], ldc,
-                                xc, _stream(dev, stream)))
+                                xc, _stream(self, dev, stream)))
 
     def moe_sort_workspace(self, tokens, topk, experts):
         """Bytes of workspace moe_sort needs (dg_moe_sort_workspace)."""
@@ -635,13 +638,14 @@ class Handle:
         _flat(offsets, "offsets", E + 1, i32, dev)
         _flat(src, "src", src.numel(), i32, dev)
         _flat(dst, "dst", T * k, i32, dev)
+        on = _stream(self, dev, stream)
         if workspace is None:
             need = self.moe_sort_workspace(T, k, E)
             if need:
                 workspace = ty.space(need, dev, stream)
         wsb = _space(workspace, dev)
         check(dg_moe_sort(self.h, T, k, E, align, ids.data_ptr(), src.numel(), offsets.data_ptr(), src.data_ptr(),
-                          dst.data_ptr(), _ptr(workspace), wsb, _stream(dev, stream)))
+                          dst.data_ptr(), _ptr(workspace), wsb, on))
 
     def moe_gather(self, X, src, Y, *, topk, stream=None):
         """Y[r] = X[src[r] // topk], zeros where src names no pair (dg_moe_gather).
@@ -654,7 +658,7 @@ class Handle:
         ldx = _rows2(X, "X", T, H, types, dev)
         ldy = _rows2(Y, "Y", R, H, (X.dtype,), dev)
         check(dg_moe_gather(self.h, R, H, X.data_ptr(), types[X.dtype], T, ldx, src.data_ptr(), topk, Y.data_ptr(),
-                            ldy, _stream(dev, stream)))
+                            ldy, _stream(self, dev, stream)))
 
     def moe_combine(self, Y, dst, O, *, weights=None, stream=None):
         """O[t] = sum over slots of weights[t, s] * Y[dst[t, s]] (dg_moe_combine);
@@ -671,7 +675,7 @@ class Handle:
         ldy = _rows2(Y, "Y", R, H, types, dev)
         ldo = _rows2(O, "O", T, H, (Y.dtype,), dev)
         check(dg_moe_combine(self.h, T, k, H, Y.data_ptr(), types[Y.dtype], R, ldy, dst.data_ptr(), _ptr(weights),
-                             O.data_ptr(), ldo, _stream(dev, stream)))
+                             O.data_ptr(), ldo, _stream(self, dev, stream)))
 
     def moe_combine_grad(self, dO, Y, dst, src, dY, dW=None, *, weights=None, stream=None):
         """Gradient of moe_combine (dg_moe_combine_grad): dY [R, H] and, unless None,
@@ -693,7 +697,7 @@ class Handle:
         lddy = _rows2(dY, "dY", R, H, (dO.dtype,), dev)
         check(dg_moe_combine_grad(self.h, T, k, H, R, dO.data_ptr(), types[dO.dtype], lddo, _ptr(Y), ldy,
                                   dst.data_ptr(), src.data_ptr(), _ptr(weights), dY.data_ptr(), lddy, _ptr(dW),
-                                  _stream(dev, stream)))
+                                  _stream(self, dev, stream)))
 
     def plan(self, M, N, K, a="f16", b="f16", c="f16", b_layout=None, epilogue="none",
              group_k=0, opts=None, **ld):
