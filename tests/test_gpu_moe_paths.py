@@ -48,3 +48,16 @@ def test_rows_20_mib_apart(h):
     unit = ref.unit_error(da, db)
     check_product(c, exact, mag, K, unit)
     check_product(want, exact, mag, K, unit)
+
+
+@pytest.mark.parametrize("N", [64, 50])
+@pytest.mark.parametrize("type", [torch.float32, torch.bfloat16])
+def test_experts_without_k(h, N, type):
+    """K = 0: zeros in the experts' rows, whatever N makes of the empty weights' stride."""
+    say(f"[case] grouped K = 0, N {N} {type}")
+    E, R = 3, 300
+    off = torch.tensor([0, 130, 130, 290], dtype=torch.int32, device=DEV)
+    a, b = (torch.empty(*s, 0, dtype=torch.uint8, device=DEV) for s in ((R,), (E, N)))
+    c = torch.full((R, N), 7.0, dtype=type, device=DEV)
+    h.gemm_fp8_grouped(a, torch.empty(0, R, device=DEV), b, torch.empty(E, 0, 1, device=DEV), off, c)
+    assert (c[:290] == 0).all() and (c[290:] == 7).all()

@@ -203,7 +203,7 @@ dg_status dg_gemm_fp8_grouped(dg_handle_t h, int64_t rows, int64_t N, int64_t K,
         Fp8Args a{};
         DG_TRY(check_out(C, c_type, a.out_type));
         if (K > 0) DG_TRY(check_operands(A, la, a_scale, B, lb, b_scale, K));
-        if (xb % 16) return api_fail(DG_ERR_ALIGNMENT, "the experts' stride of B is a multiple of 16");
+        if (K > 0 && xb % 16) return api_fail(DG_ERR_ALIGNMENT, "the experts' stride of B is a multiple of 16");
         if (!aligned(offsets, 4)) return api_fail(DG_ERR_ALIGNMENT, "offsets are 4-byte aligned");
         a.A = A, a.B = B, a.sa = a_scale, a.sb = b_scale, a.C = C, a.off = offsets;
         a.lda = la, a.ldb = lb, a.ld_sa = lsa, a.ld_sb = lsb, a.ldc = lc, a.stride_b = xb, a.stride_sb = xs;
