@@ -344,12 +344,15 @@ class _Types:
         self.torch = torch
 
     def space(self, nbytes, device, stream):
-        """A workspace allocated for one call; kept from reuse until `stream` is past it."""
-        t = self.torch.empty(nbytes, dtype=self.torch.uint8, device=device)
-        if stream is not None:
-            cuda = self.torch.cuda
-            t.record_stream(cuda.ExternalStream(stream, device=device) if stream else cuda.default_stream(device))
-        return t
+        """A workspace allocated for one call, out of the memory of the stream the call
+        runs on: what else ever held or will hold it is ordered with the call.
+        (Another stream's memory may be in use by work still enqueued there.)"""
+        torch = self.torch
+        if stream is None or stream == self.current_stream(device.index):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        cuda = torch.cuda
+        with cuda.stream(cuda.ExternalStream(stream, device=device) if stream else cuda.default_stream(device)):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 _types_once = None
