@@ -424,9 +424,12 @@ dg_status dg_plan_fp8(dg_handle_t h, int64_t M, int64_t N, int64_t K, dg_plan_in
  *   C[i][j] = sum over blocks g of a_scale[g][i] * b_scale[g][j / b_block] *
  *             (sum over k in block g of A[i][k] * B[j][k])
  * accumulated in binary32 and rounded once to C's type; the two scales of a block are
- * multiplied first, in binary32.  With a 16-bit C the
- * block sums may come from the fp8 MFMA, which cuts products below 2^-13 of the
- * largest among 8 consecutive k; with an F32 C every product is exact.
+ * multiplied first, in binary32.  With an F32 C every product is exact.  With a 16-bit
+ * C the block sums come from the fp8 MFMA (but for dense products of up to 16 rows),
+ * which inside each 8 consecutive k cuts products towards zero at 2^-13 of the largest:
+ * 1.4e-5 of the result's norm on normal values, more of an element whose terms cancel.
+ * The order of the sums follows from the sizes and from a row's place among the rows:
+ * equal rows at different places may differ in their last bits.
  *   A        device, e4m3 codes M x K (lda bytes); B N x K (ldb bytes): 16-byte
  *            aligned, rows multiples of 16 bytes and readable to their end (bytes at
  *            and past K may hold anything); any K

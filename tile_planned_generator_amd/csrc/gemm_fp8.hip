@@ -12,11 +12,13 @@
 //
 // Two ways to compute P_g of a 16 x 16 tile:
 //   - one 16x16x128 fp8 MFMA.  Inside each group of 8 consecutive k its adder cuts
-//     products at 2^-13 of the group's largest (probed: a product 2^-14 of its
-//     neighbour adds nothing, while across groups all 24 bits survive): an error
-//     of 1.5e-5 of the result's norm on normal values.  Outputs of 16 bits are
-//     rounded 100 times coarser (2^-9 or 2^-12 of each value), so the tiled kernel
-//     takes it for them.
+//     every product towards zero at 2^-13 of the group's largest (exactly so:
+//     tests/test_gpu_fp8_unit.py; across groups all 24 bits survive): an error of
+//     1.4e-5 of the result's norm on normal values, 2.9e-5 with a few columns 16 times
+//     the others.  Rounding the result is 120 (bf16, 1.7e-3) or 15 (f16, 2.1e-4) times
+//     coarser, so the tiled kernel takes it for outputs of 16 bits.  The error goes
+//     with the products' magnitudes, not with the value: an element whose terms
+//     cancel may lose more than its own rounding (an F32 output does not).
 //   - EXACT: both operands widened to binary16 (every e4m3 value is one) and four
 //     chained 16x16x32 binary16 MFMAs, whose products are exact and whose sums are
 //     kept in binary32, at half the rate: for binary32 outputs, and everywhere in
@@ -174,7 +176,8 @@ __global__ void __launch_bounds__(WM *WN * 64, 2) fp8_tiled_kernel(Fp8Args p)
     const int L16 = lane & 15, g16 = lane >> 4;
 
     // ---- the tile: consecutive workgroups of a die take consecutive tiles, four
-    // row tiles (of one expert) side by side
+    // row tiles side by side (over experts the next four in the list of all row
+    // tiles, which may belong to two experts)
     int m0, mend, n0, expert = 0, kbeg = 0, kend = p.K;
     {
         int T, t, e_rows = p.tiles_m;

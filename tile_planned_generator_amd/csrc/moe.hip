@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeMoveArgs p)
 
 // Gradient of the combination: out[dst[t][s]] = w[t][s] dout[t] and
 // dw[t][s] = <x[dst[t][s]], dout[t]>.  Wave u takes pair u, whose row it walks in
-// runs of 2048 columns with all loads of a run in flight, and then clears row u
+// runs of 2048 columns (1024 of binary32) with all loads of a run in flight, and then clears row u
 // (and u + waves, ...) if no pair has it.  7108 rows of 1112 f16: 7.8 us (36 MB, 4.5
 // TB/s; one workgroup per pair, and 64 empty rows to a wave, took 24.7).
 template <typename T>
