@@ -317,11 +317,13 @@ def _dtype_name(t):
 def _stream(h, device, stream):
     """The HIP stream of a call through handle h: `stream`, or the current stream of
     the operands' `device`, which has to be the handle's."""
-    if device.type != "cuda":
-        raise ValueError(f"the operands are on {device}, not on a GPU")
-    if h.index is not None and device.index != h.index:
-        raise ValueError(f"the operands are on {device}, the handle is cuda:{h.index}'s")
-    return _types().current_stream(device.index) if stream is None else stream
+    index = device.index
+    if index is None or index != h.index:   # (an offline handle has none: the library refuses it)
+        if device.type != "cuda":
+            raise ValueError(f"the operands are on {device}, not on a GPU")
+        if h.index is not None:
+            raise ValueError(f"the operands are on {device}, the handle is cuda:{h.index}'s")
+    return _types().current_stream(index) if stream is None else stream
 
 
 def _ptr(t):
