@@ -6,6 +6,7 @@ import torch
 
 from tests.parity import say
 from tests.test_gpu_moe import DEV, codes, gen, h, scales  # noqa: F401 (h: fixture)
+from tile_planned_generator_amd import dg
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +24,15 @@ def sort(h):
     out = torch.zeros(65 + 20000, dtype=torch.int32, device=DEV)
     return (lambda s: h.moe_sort(ids, out[:65], out[65:10065], out[10065:].view(5000, 2), stream=s)), out, \
         h.moe_sort_workspace(5000, 2, 64)
+
+
+def planned(h):
+    """A planned product cut along K (dg_gemm)."""
+    g, (M, N, K) = gen(83), (192, 160, 512)
+    a, b = (torch.randn(*s, generator=g).half().to(DEV) for s in ((M, K), (K, N)))
+    out, opts = torch.zeros(M, N, dtype=torch.float16, device=DEV), dg.dg_plan_opts(force_split_k=2, force_path=dg.DG_PATH_TILED)
+    return (lambda s: h.gemm(a, b, out, opts=opts, stream=s)), out, \
+        h.plan(M, N, K, opts=opts).workspace_bytes
 
 
 class Busy:
@@ -54,7 +64,7 @@ def result(call, out):
     return want
 
 
-@pytest.mark.parametrize("make", [gemm, sort])
+@pytest.mark.parametrize("make", [gemm, sort, planned])
 def test_memory_that_earlier_work_still_reads(h, busy, make):
     say(f"[case] own workspace, memory in use: {make.__name__}")
     call, out, need = make(h)
@@ -72,7 +82,7 @@ def test_memory_that_earlier_work_still_reads(h, busy, make):
     assert all((c == 7).all() for c in copies) and torch.equal(out, want)
 
 
-@pytest.mark.parametrize("make", [gemm, sort])
+@pytest.mark.parametrize("make", [gemm, sort, planned])
 @pytest.mark.parametrize("default", [False, True])
 def test_memory_that_is_handed_out_after_the_call(h, busy, make, default):
     """`default`: the call names stream 0 while another stream is current."""

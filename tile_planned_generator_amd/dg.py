@@ -352,7 +352,7 @@ class _Types:
         torch = self.torch
         if stream is None or stream == self.current_stream(device.index):
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        cuda = torch.cuda
+        cuda, stream = torch.cuda, getattr(stream, "value", stream) or 0   # (a ctypes pointer has its value there)
         with cuda.stream(cuda.ExternalStream(stream, device=device) if stream else cuda.default_stream(device)):
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
@@ -503,7 +503,7 @@ class Handle:
         info = self.plan(M, N, K, "f8e4m3", "e2m1", c, DG_COL_MAJOR, epilogue, group_k=32, opts=opts,
                          lda=lda, ldb=ldb, ldc=ldc)
         if workspace is None and info.workspace_bytes > 0:
-            workspace = torch.empty(info.workspace_bytes, dtype=torch.uint8, device=A.device)
+            workspace = _types().space(info.workspace_bytes, A.device, stream)
         ws_ptr = workspace.data_ptr() if workspace is not None else None
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
         if stream is None:
@@ -799,7 +799,7 @@ class Handle:
         info = self.plan(M, N, K, a, b, c, b_layout, epilogue, opts=opts, lda=lda, ldb=ldb,
                          ldc=ldc, ldd=ldd)
         if workspace is None and info.workspace_bytes > 0:
-            workspace = torch.empty(info.workspace_bytes, dtype=torch.uint8, device=A.device)
+            workspace = _types().space(info.workspace_bytes, A.device, stream)
         ws_ptr = workspace.data_ptr() if workspace is not None else None
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
         args = (self.h, M, N, K, C.byref(dt), C.byref(lay), A.data_ptr(), B.data_ptr(),
