@@ -28,7 +28,8 @@
 // fp8 and 1.44 in bfloat16): 4096^3 to bf16 61.5 us (2.24 PFLOP/s) and to f32 114-126
 // us; 8192 rows over 8 experts of 4096 x 4096 155-182 us as the rows fall; their
 // weight gradients (2048 x 4096, f32) 165 us, of which writing 268 MB is 54; 32 rows
-// over 8 experts 26.3 us (5.1 TB/s of weights); one token through 4096 x 4096 6.0 us.
+// over 8 experts 20.8-26.3 us (5.1 TB/s of weights at 26.3); one token through 4096 x
+// 4096 6.2 us.
 #include "gemm_tiled.h"
 #include "launch.h"
 #include "moe_args.h"
@@ -139,7 +140,7 @@ DG_DEV void seg_find(const int32_t *off, int experts, int rows, int bm, int t, i
 
 // ---------------------------------------------------------------- tiled kernel
 // What bounds it (256 x 256, 4096^3): a step of 128 takes 1.56 us where its MFMAs
-// take 0.94 at the clock it ran at (2.17 GHz, counters: matrix unit 49 % busy while
+// take 0.94 at the clock it ran at (2.17 GHz, counters: matrix unit 56 % busy while
 // the CU is, no LDS conflicts to speak of).  In timing copies the step took 1.29 us
 // without the loads, 1.37 without the scaling FMAs and 1.12 without both: the three
 // share the issue of two waves per SIMD.  Four MFMAs and then sixteen FMAs, or
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(WM *WN * 64, 2) fp8_tiled_kernel(Fp8Args p)
 // 16 FN columns and cuts K over its NW waves (wave w takes blocks w, w + NW, ...),
 // operands go from memory to registers, and the waves' sums are added in wave
 // order through LDS: no workspace, and the same result on every run.  One row, N = K =
-// 4096: 6.0 us (2.8 TB/s, mostly latency: each wave has one batch of loads);
+// 4096: 6.2 us (2.7 TB/s, mostly latency: each wave has one batch of loads);
 // 64 x 64 tiles with a K split and its sum took 3 us more.
 template <int FM, int FN, int NW, int MODE, bool BB1>
 __global__ void __launch_bounds__(NW * 64) fp8_stream_kernel(Fp8Args p)
