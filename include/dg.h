@@ -390,9 +390,10 @@ dg_status dg_quant_mx(dg_handle_t h, int64_t M, int64_t K, const void *X, int64_
  * nothing and reports argument errors before anything is enqueued
  * (DG_ERR_INVALID_STATE, DG_ERR_INVALID_ARG, DG_ERR_UNSUPPORTED,
  * DG_ERR_ALIGNMENT, DG_ERR_WORKSPACE, DG_ERR_HIP); a leading dimension or stride of
- * 0 means tightly packed; results are the same on every run.  Index arrays and offsets live on the
- * device and are not checked by the host: entries out of range are read as "no
- * row", and offsets are clamped, so no access leaves the operands. */
+ * 0 means tightly packed; sizes reach 2^31-4096; results are the same on every run.
+ * Index arrays and offsets live on the device and are not checked by the host: entries
+ * out of range are read as "no row", and offsets are clamped, so no access leaves the
+ * operands. */
 
 /* fp8 quantiser.  Per block of 128 consecutive values: scale =
  * max(max|x| / 448, 2^-126), code = e4m3(x / scale), both divisions rounded to

@@ -8,6 +8,9 @@
 namespace dg {
 
 constexpr int FP8_BLOCK = 128;   // values along K that share a scale
+// The largest size of the expert layer's calls: launchers and kernels round sizes up to
+// whole tiles, blocks and runs (of 2048 columns at most) in 32 bits.
+constexpr int64_t FP8_MOST = INT32_MAX - 4095;
 // Kernel variants of the product (indices of the tables in gemm_fp8.hip).
 enum Fp8Kernel : int { FP8_STREAM16 = 0, FP8_TILE64, FP8_TILE128, FP8_TILE256, FP8_KERNELS };
 

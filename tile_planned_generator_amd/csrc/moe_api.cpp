@@ -39,7 +39,7 @@ dg_status sizes_ok(std::initializer_list<int64_t> sizes)
 {
     for (int64_t v : sizes) {
         if (v < 0) return api_fail(DG_ERR_INVALID_ARG, "negative size or leading dimension");
-        if (v > INT32_MAX) return api_fail(DG_ERR_UNSUPPORTED, "sizes above 2^31-1 are not supported");
+        if (v > FP8_MOST) return api_fail(DG_ERR_UNSUPPORTED, "sizes above 2^31-4096 are not supported");
     }
     return DG_OK;
 }
@@ -278,8 +278,8 @@ dg_status dg_moe_sort(dg_handle_t h, int64_t tokens, int64_t topk, int64_t exper
         if (experts > MOE_MAX_EXPERTS) return api_fail(DG_ERR_UNSUPPORTED, "more than 512 experts");
         const int64_t pairs = tokens * topk;
         // every expert that has a pair may round up
-        if (pairs + std::min(pairs, experts) * (align - 1) > INT32_MAX)
-            return api_fail(DG_ERR_UNSUPPORTED, "sizes above 2^31-1 are not supported");
+        if (pairs + std::min(pairs, experts) * (align - 1) > FP8_MOST)
+            return api_fail(DG_ERR_UNSUPPORTED, "sizes above 2^31-4096 are not supported");
         if (capacity < pairs + std::min(pairs, experts) * (align - 1))
             return api_fail(DG_ERR_INVALID_ARG, "capacity does not hold every expert's rows rounded up to align");
         if (!offsets || (pairs > 0 && (!ids || !dst)) || (capacity > 0 && !src))
