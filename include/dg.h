@@ -390,7 +390,9 @@ dg_status dg_quant_mx(dg_handle_t h, int64_t M, int64_t K, const void *X, int64_
  * nothing and reports argument errors before anything is enqueued
  * (DG_ERR_INVALID_STATE, DG_ERR_INVALID_ARG, DG_ERR_UNSUPPORTED,
  * DG_ERR_ALIGNMENT, DG_ERR_WORKSPACE, DG_ERR_HIP); a leading dimension or stride of
- * 0 means tightly packed; sizes reach 2^31-4096; results are the same on every run.
+ * 0 means tightly packed; sizes reach 2^31-4096, as far as one launch's 2^32 work-items
+ * do (DG_ERR_UNSUPPORTED past them: 2^26 rows of up to 512 columns moved, 2^26 pairs or
+ * rows of a gradient); results are the same on every run.
  * Index arrays and offsets live on the device and are not checked by the host: entries
  * out of range are read as "no row", and offsets are clamped, so no access leaves the
  * operands. */

@@ -12,6 +12,7 @@ SHIM = """
 extern "C" {
 int experts_disjoint(int64_t M, int64_t N, int64_t ld, int64_t stride, int64_t experts)
 { return dg::experts_disjoint(M, N, ld, stride, experts); }
+int grid_fits(int64_t workgroups, int threads, int64_t times) { return dg::grid_fits((__int128)workgroups * times, threads); }
 int rows_fit_32(int rows, int64_t ld, int64_t K) { return dg::rows_fit_32(rows, ld, K); }
 int choose_dense(int64_t M, int64_t N, int64_t K, int exact, int64_t lda, int64_t ldb)
 { return dg::choose_dense(M, N, K, dg::huge_tile(exact, lda, ldb, K)).kernel; }
@@ -33,6 +34,7 @@ def lib():
         subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I" + CSRC, src, "-o", so], check=True)
         loaded = C.CDLL(so)
     loaded.experts_disjoint.argtypes = [C.c_int64] * 5
+    loaded.grid_fits.argtypes = [C.c_int64, C.c_int, C.c_int64]
     loaded.rows_fit_32.argtypes = [C.c_int, C.c_int64, C.c_int64]
     for choose in (loaded.choose_dense, loaded.choose_rows, loaded.choose_wgrad):
         choose.argtypes = [C.c_int64] * 3 + [C.c_int, C.c_int64, C.c_int64]

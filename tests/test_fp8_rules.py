@@ -40,3 +40,13 @@ def test_wide_rows_leave_the_256_tile(which):
         assert rows(256, 1, 49152, 0, **{which: ld}) == tile
         assert wgrad(256, 256, 192, 0, **{which: ld}) == tile
     assert dense(256, 49152, 2 ** 24 - 16, 0, lda=2 ** 24 - 16, ldb=2 ** 24 - 16) == fp8_rules.TILE128   # (K counts too)
+
+
+def test_launches_of_up_to_32_bits_of_work_items():
+    fits = fp8_rules.lib().grid_fits
+    for threads in (256, 512, 1024):
+        most = (LIMIT - 1) // threads
+        assert fits(most, threads, 1) and fits(1, threads, 1)
+        for workgroups, times in ((most + 1, 1), (2 ** 31 - 1, 1), (2 ** 32 // threads * 3, 1), (2 ** 62, 1),
+                                  (2 ** 50, 2 ** 14), (2 ** 50, 2 ** 31 - 1)):   # (a product that passes 64 bits)
+            assert not fits(workgroups, threads, times), (workgroups, times)

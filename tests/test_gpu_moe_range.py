@@ -6,6 +6,7 @@ import torch
 from tests import moe_ref as ref
 from tests.parity import say
 from tests.test_gpu_moe import DEV, F8, gen, h  # noqa: F401 (h: fixture)
+from tile_planned_generator_amd import dg
 
 pytestmark = pytest.mark.gpu
 ROWS, H = 1 << 21, 2056     # 4.3e9 elements
@@ -53,7 +54,8 @@ def test_movement(h, rows):
     assert torch.equal(dy[at], grad)
     dy[at] = 0
     assert not any(part.any() for part in dy.split(1 << 18))
-    assert torch.equal(dw.double().view(-1)[live], (want[live].double() * do[torch.tensor(live, device=DEV) // k].double()).sum(1))
+    terms = want[live].double() * do[torch.tensor(live, device=DEV) // k].double()
+    assert torch.equal(dw.double().view(-1)[live], terms.sum(1))
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -82,7 +84,8 @@ def test_experts(h):
     b[-1] = last.to(F8).to(DEV)
     x = torch.randint(-3, 4, (R, K), generator=g).float()
     c = torch.full((R, N), 7.0, device=DEV)
-    h.gemm_fp8_grouped(x.to(F8).to(DEV), torch.ones(K // 128, R, device=DEV), b, torch.ones(E, K // 128, N // 128, device=DEV), off, c)
+    h.gemm_fp8_grouped(x.to(F8).to(DEV), torch.ones(K // 128, R, device=DEV), b,
+                       torch.ones(E, K // 128, N // 128, device=DEV), off, c)
     want = x[-128:].to(DEV) @ last.t().contiguous().to(DEV)     # whole numbers below 2^24
     assert torch.equal(c[-128:], want) and not c[:-128].any()
     del b, c
@@ -96,3 +99,20 @@ def test_experts(h):
             assert torch.equal(dw[e], (dy[:, seg].to(DEV) @ x[seg].to(DEV)).to(t))
         del dw
     torch.cuda.empty_cache()
+
+
+def test_the_largest_launch(h):
+    """A wave moves a row's piece: 2^26 of them pass one launch's 2^32 work-items, and are refused."""
+    most, H = (1 << 26) - 4, 2
+    say(f"[case] gather of {most} rows")
+    x = torch.arange(12, dtype=torch.bfloat16, device=DEV).view(6, H)
+    src = torch.randint(-1, 6, (most + 4,), generator=torch.Generator(device=DEV).manual_seed(5), dtype=torch.int32, device=DEV)
+    y = torch.full((most + 4, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(dg.DGError) as e:
+        h.moe_gather(x, src, y, topk=1)
+    assert e.value.status == dg.DG_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert (y == 7).all()
+    h.moe_gather(x, src[:most], y[:most], topk=1)
+    want = torch.cat([torch.zeros(1, H, dtype=torch.bfloat16, device=DEV), x])[src[:most].long() + 1]
+    assert torch.equal(y[:most], want) and (y[most:] == 7).all()

@@ -14,6 +14,10 @@ constexpr int64_t FP8_MOST = INT32_MAX - 4095;
 // Kernel variants of the product (indices of the tables in gemm_fp8.hip).
 enum Fp8Kernel : int { FP8_STREAM16 = 0, FP8_TILE64, FP8_TILE128, FP8_TILE256, FP8_KERNELS };
 
+// Whether one launch takes so many workgroups: HIP counts a launch's work-items in 32
+// bits along x.  (128 bits: tiles times experts may pass 64.)
+inline bool grid_fits(__int128 workgroups, int threads) { return workgroups * threads < (__int128)1 << 32; }
+
 inline int64_t blocks_of(int64_t n) { return (n + FP8_BLOCK - 1) / FP8_BLOCK; }
 
 struct Fp8Choice {

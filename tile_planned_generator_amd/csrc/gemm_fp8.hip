@@ -667,9 +667,10 @@ hipError_t launch_fp8(int kernel, int mode, int b_block, const Fp8Args &a, hipSt
         arg.tiles_m = (a.M + sh.bm - 1) / sh.bm;
     }
     const int64_t tiles = (int64_t)arg.tiles_m * arg.tiles_n;
-    const int64_t grid = mode == FP8_WGRAD ? (tiles + 7) / 8 * 8 * a.experts : tiles;   // (whole turns of the 8 dies per expert)
+    const __int128 grid = mode == FP8_WGRAD ? (__int128)((tiles + 7) / 8 * 8) * a.experts : tiles;   // (whole turns of the 8 dies per expert)
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff || arg.split_k < 1 || arg.split_k > 65535) return hipErrorInvalidValue;
+    if (!grid_fits(grid, sh.threads)) return hipErrorInvalidConfiguration;
+    if (arg.split_k < 1 || arg.split_k > 65535) return hipErrorInvalidValue;
     void *args[] = {&arg};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)grid, (unsigned)arg.split_k, 1), dim3(sh.threads, 1, 1), args, 0, s);
     return e != hipSuccess ? e : hipGetLastError();

@@ -306,7 +306,7 @@ namespace {
 hipError_t launch_move(const void *f16, const void *bf16, const void *f32, const MoeMoveArgs &a, int64_t grid, hipStream_t s)
 {
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidConfiguration;
     MoeMoveArgs arg = a;
     void *args[] = {&arg};
     const void *fn = a.type == T_F16 ? f16 : (a.type == T_BF16 ? bf16 : f32);

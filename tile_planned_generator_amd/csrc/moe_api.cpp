@@ -32,6 +32,8 @@ dg_status device_ready(dg_handle_t h)
 
 dg_status launched(hipError_t e)
 {
+    if (e == hipErrorInvalidConfiguration)
+        return api_fail(DG_ERR_UNSUPPORTED, "the problem takes 2^32 work-items or more, one launch's limit");
     return e == hipSuccess ? DG_OK : api_fail(DG_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
 }
 

@@ -237,7 +237,7 @@ hipError_t launch_quant_fp8(const QuantFp8Args &a, bool transpose, hipStream_t s
     const int64_t grid = transpose ? ((int64_t)a.rows + FP8_BLOCK - 1) / FP8_BLOCK * ((a.cols + QC_COLS - 1) / QC_COLS)
                                    : ((int64_t)a.rows + QR_ROWS - 1) / QR_ROWS * ((a.cols + QR_COLS - 1) / QR_COLS);
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidConfiguration;
     const void *fn;
     if (a.x_type == T_F16) fn = transpose ? (const void *)quant_fp8_cols_kernel<_Float16> : (const void *)quant_fp8_rows_kernel<_Float16>;
     else if (a.x_type == T_BF16) fn = transpose ? (const void *)quant_fp8_cols_kernel<__bf16> : (const void *)quant_fp8_rows_kernel<__bf16>;
